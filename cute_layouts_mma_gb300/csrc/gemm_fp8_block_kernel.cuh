@@ -727,6 +727,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                         if (n < p.N) {
                             if (ok) ok = wait(c_bar(i), cph >> buf & 1u);
                             cph ^= 1u << buf;
+                        } else {
+                            // no C comes past the columns, and so no wait with it: an earlier box may
+                            // still be leaving this buffer, which the sums are written to all the same
+                            if (lane == 0) bulk_wait_group_read<0>();
+                            __syncwarp();
                         }
                     } else {
                         // (boxes are one group per buffer, in turn; the lanes' passes are none, so
