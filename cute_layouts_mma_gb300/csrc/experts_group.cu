@@ -32,8 +32,10 @@ constexpr int kPlaceWarps = 16;
 constexpr int kSingleWarps = 32;
 constexpr int kScanWarps = 8;
 
-// The last block takes the rest, so every block has at least kChunk pairs.
-__device__ __forceinline__ int block_end(int b, int blocks, int n) { return b == blocks - 1 ? n : (b + 1) * kChunk; }
+// Pairs of block b, from pair b * kChunk on.  The last block takes the rest, so every block has
+// at least kChunk.  Places within a block are counted from its first pair: up to 2^31 - 1 pairs
+// fit an int, a step past the last of them does not.
+__device__ __forceinline__ int block_pairs(int b, int blocks, int n) { return b == blocks - 1 ? n - b * kChunk : kChunk; }
 
 __global__ void __launch_bounds__(kCountThreads) count_kernel(const int32_t* ids, int32_t* position, int n, int E, int blocks) {
     __shared__ int count[kMaxExperts];
@@ -41,10 +43,10 @@ __global__ void __launch_bounds__(kCountThreads) count_kernel(const int32_t* ids
     griddep_launch_dependents();
     griddep_wait();
     __syncthreads();
-    const int b = blockIdx.x, begin = b * kChunk, end = block_end(b, blocks, n);
+    const int b = blockIdx.x, begin = b * kChunk, own = block_pairs(b, blocks, n);
 #pragma unroll 8
-    for (int i = begin + static_cast<int>(threadIdx.x); i < end; i += kCountThreads) {
-        const unsigned e = static_cast<unsigned>(ids[i]);
+    for (int i = threadIdx.x; i < own; i += kCountThreads) {
+        const unsigned e = static_cast<unsigned>(ids[begin + i]);
         if (e < static_cast<unsigned>(E)) atomicAdd(&count[e], 1);
     }
     __syncthreads();
@@ -141,9 +143,9 @@ __global__ void __launch_bounds__(WARPS * 32)
     for (int i = threadIdx.x; i < WARPS * E; i += kThreads) count[i] = 0;
     griddep_launch_dependents();
     griddep_wait();
-    const int b = blockIdx.x, begin = SINGLE ? 0 : b * kChunk, end = SINGLE ? n : block_end(b, blocks, n);
-    const int per = ((end - begin + kThreads - 1) / kThreads) * 32;  // pairs per warp, whole groups of 32
-    const int w0 = begin + warp * per, w1 = min(end, w0 + per);
+    const int b = blockIdx.x, begin = SINGLE ? 0 : b * kChunk, pairs = SINGLE ? n : block_pairs(b, blocks, n);
+    const int per = ((pairs + kThreads - 1) / kThreads) * 32;  // pairs per warp, whole groups of 32
+    const int w0 = warp * per, w1 = min(pairs, w0 + per);
     int* row = count + warp * E;
     int* shift = count + WARPS * E;                  // not SINGLE: [E], from the block's order to all blocks'
     int* sorted = shift + (SINGLE ? 0 : E);          // [n or kPairs], the pairs in the block's order
@@ -152,7 +154,7 @@ __global__ void __launch_bounds__(WARPS * 32)
     unsigned id[PER];
     int at[PER];  // place within the warp's pairs of the expert
 #pragma unroll
-    for (int j = 0; j < PER; ++j) id[j] = w0 + j * 32 + lane < w1 ? static_cast<unsigned>(ids[w0 + j * 32 + lane]) : 0xffffffffu;
+    for (int j = 0; j < PER; ++j) id[j] = w0 + j * 32 + lane < w1 ? static_cast<unsigned>(ids[begin + w0 + j * 32 + lane]) : 0xffffffffu;
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
@@ -206,17 +208,17 @@ __global__ void __launch_bounds__(WARPS * 32)
             if (id[j] < static_cast<unsigned>(E)) {
                 const int own = row[id[j]] + at[j];
                 to = SINGLE ? own : own + shift[id[j]];
-                sorted[own] = i;
+                sorted[own] = begin + i;
                 if (!SINGLE) target[own] = to;
             }
-            position[i] = to;
+            position[begin + i] = to;
         }
     }
     // The order goes through shared memory: a store whose lanes are scattered takes a cycle per
     // lane of the SM's one store path, one of runs (a run is a block's pairs of one expert) few.
     __syncthreads();
     for (int i = threadIdx.x; i < mine; i += kThreads) order[SINGLE ? i : target[i]] = sorted[i];
-    for (int i = max(begin, all) + static_cast<int>(threadIdx.x); i < end; i += kThreads) order[i] = -1;
+    for (int i = min(max(all - begin, 0), pairs) + static_cast<int>(threadIdx.x); i < pairs; i += kThreads) order[begin + i] = -1;
 }
 
 }  // namespace

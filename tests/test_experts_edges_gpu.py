@@ -55,3 +55,38 @@ def test_gemm_another_c_and_infinite_rows_at_a_column_remainder(M, N, K, scales)
         assert torch.equal(torch.isnan(D[:M]), torch.isnan(want))
         assert torch.equal(torch.nan_to_num(D[:M], nan=0.0), torch.nan_to_num(want, nan=0.0))
         assert (D[M:] == 12345.0).all()
+
+
+# ------------------------------------------------------------------ grouping
+
+@pytest.mark.parametrize("n", [2 ** 31 - 1, 2 ** 31 - 400, 2 ** 31 - 513])
+@pytest.mark.parametrize("dropped", [0, 1])
+def test_group_of_nearly_two_to_the_31_pairs(n, dropped):
+    """The largest pair counts: ids repeat in turn, so each place has a formula."""
+    dev = _dev()
+    if torch.cuda.mem_get_info(dev)[0] < 36 << 30:
+        pytest.skip("26 GB of pairs")
+    E = 3
+    period = E + 2 * dropped  # -1 and E are no experts
+    counts = [(n - (e + dropped) + period - 1) // period for e in range(E)]
+    first = [sum(counts[:e]) for e in range(E + 1)]
+    ids = torch.empty(n, 1, dtype=torch.int32, device=dev)
+    step = 1 << 27
+    for lo in range(0, n, step):
+        hi = min(n, lo + step)
+        ids[lo:hi, 0] = torch.arange(lo, hi, device=dev) % period - dropped
+    offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    order, position = (torch.full((n,), 5, dtype=torch.int32, device=dev) for _ in range(2))
+    tg.expert_group(ids, offsets, order, position)
+    _done()
+    assert offsets.tolist() == first
+    start = torch.tensor(first[:E], device=dev)
+    for lo in range(0, n, step):
+        hi = min(n, lo + step)
+        p = torch.arange(lo, hi, device=dev)
+        e = p % period - dropped
+        place = torch.where((e >= 0) & (e < E), start[e.clamp(0, E - 1)] + p // period, -1)
+        assert torch.equal(position[lo:hi].long(), place)
+        e = torch.bucketize(p, torch.tensor(first[1:], device=dev), right=True)  # of the place
+        pair = torch.where(e < E, (p - start[e.clamp(max=E - 1)]) * period + e + dropped, -1)
+        assert torch.equal(order[lo:hi].long(), pair)
