@@ -73,7 +73,8 @@ struct RowsParams {
     uint8_t* Q;
     float* SF;
     int64_t M, ld, R;
-    int K, blocks;
+    uint32_t K;  // below 2^31: a segment's end, and the step to the next, fit 32 bits without a sign
+    int blocks;
     int index_div;
 };
 
@@ -126,9 +127,9 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsParams p) {
     }
     const T* x_row = static_cast<const T*>(p.X) + (src < 0 ? 0 : src * p.ld);
     uint8_t* q_row = p.Q + row * p.K;
-    auto segment = [&](const int seg, auto whole) {
+    auto segment = [&](const uint32_t seg, auto whole) {
         constexpr bool kWhole = decltype(whole)::value;  // every element of the segment is there
-        const int k0 = seg * (U * 256) + lane * 8;
+        const uint32_t k0 = seg * (U * 256) + lane * 8;
         Eight<T> x[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -157,7 +158,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsParams p) {
             }
         }
         const float factor = block_factor(a[0]);
-        const int block = seg * (U * 2) + 2 * piece + (lane >> 4);
+        const int block = static_cast<int>(seg * (U * 2)) + 2 * piece + (lane >> 4);
         // of the 16 / U lanes that hold a block, the first writes its scale
         if ((l & (16 / U - 1)) == 0 && block < p.blocks) p.SF[row * p.blocks + block] = block_scale(a[0]);
 #pragma unroll
@@ -172,7 +173,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsParams p) {
                     make_uint2(codes4(v[0].x, v[0].y, v[1].x, v[1].y), codes4(v[2].x, v[2].y, v[3].x, v[3].y));
         }
     };
-    for (int seg = blockIdx.y; seg * (U * 256) < p.K; seg += gridDim.y) {
+    for (uint32_t seg = blockIdx.y; seg * (U * 256) < p.K; seg += gridDim.y) {
         if (src >= 0 && (seg + 1) * (U * 256) <= p.K)
             segment(seg, std::true_type{});
         else
@@ -298,7 +299,7 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const TileParams p) {
 
 template <class T, int U>
 cudaError_t launch_rows_of(const RowsParams& p, int64_t warps, cudaStream_t stream) {
-    const int64_t segs = (p.K + U * 256 - 1) / (U * 256);
+    const int64_t segs = (int64_t(p.K) + U * 256 - 1) / (U * 256);
     int64_t y = (warps + p.R - 1) / p.R;  // segments side by side until there are `warps` warps
     y = y < segs ? y : segs;
     const int64_t x = (p.R + kThreads / 32 - 1) / (kThreads / 32);
@@ -312,7 +313,7 @@ cudaError_t launch_rows(const RowsParams& p, int sms, cudaStream_t stream) {
     // flight per lane), while that leaves eight warps per SM: few rows are cut finer.  1, 2, 4, 8
     // pieces (us): 4096 x 8192 26.7, 17.8, 13.9, 13.3; 1024 x 8192 7.1, 5.3, 4.1, 4.3; smaller
     // calls are within the launch's 3.7.
-    const int64_t pieces = (p.K + 255) / 256, warps = int64_t(sms) * 8;
+    const int64_t pieces = (int64_t(p.K) + 255) / 256, warps = int64_t(sms) * 8;
     auto fits = [&](int u) { return pieces >= u && p.R * ((pieces + u - 1) / u) >= warps; };
     if (fits(8)) return launch_rows_of<T, 8>(p, 4 * warps, stream);
     if (fits(4)) return launch_rows_of<T, 4>(p, 4 * warps, stream);
@@ -369,7 +370,7 @@ extern "C" gemm_status_t quantize_fp8(int64_t M, int64_t K, const void* X, int64
         p.M = M;
         p.ld = ld;
         p.R = R;
-        p.K = static_cast<int>(K);
+        p.K = static_cast<uint32_t>(K);
         p.blocks = static_cast<int>(kb);
         p.index_div = static_cast<int>(index_div);
         e = dtype == GEMM_DT_F32    ? launch_rows<float>(p, sms, stream)

@@ -90,3 +90,41 @@ def test_group_of_nearly_two_to_the_31_pairs(n, dropped):
         e = torch.bucketize(p, torch.tensor(first[1:], device=dev), right=True)  # of the place
         pair = torch.where(e < E, (p - start[e.clamp(max=E - 1)]) * period + e + dropped, -1)
         assert torch.equal(order[lo:hi].long(), pair)
+
+
+# ------------------------------------------------------------------ quantisation
+
+def _rows_formula(x):
+    """Codes and scales of FP8_ROWS by the definition in fp32 (no NaN or infinity), on x's device."""
+    b = torch.nn.functional.pad(x.float(), (0, -x.shape[1] % 128)).unflatten(1, (-1, 128))
+    a = b.abs().amax(dim=2, keepdim=True).clamp_min(X.FLOOR)
+    most = torch.full_like(a, 448.0)
+    q = (b * (most / a)).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    return q.flatten(1)[:, :x.shape[1]], (a / most)[:, :, 0]
+
+
+@pytest.mark.parametrize("dtype,K,index", [("bfloat16", 2 ** 31 - 144, None), ("bfloat16", 2 ** 31 - 2064, [0, -1]), ("float32", 2 ** 31 - 1040, [0, 0])])
+def test_quantize_rows_of_nearly_two_to_the_31_elements(dtype, K, index):
+    dev = _dev()
+    if torch.cuda.mem_get_info(dev)[0] < 40 << 30:
+        pytest.skip("rows of 2^31 elements")
+    g = torch.Generator(device=dev).manual_seed(3)
+    x = torch.empty(1, K, dtype=getattr(torch, dtype), device=dev)
+    step = 1 << 27  # whole blocks
+    for lo in range(0, K, step):
+        x[:, lo:lo + step].normal_(generator=g)
+    R = 1 if index is None else len(index)
+    q = torch.full((R + 1, K), 99, dtype=torch.uint8, device=dev)
+    sf = torch.full((R + 1, X.blocks(K)), -1.0, device=dev)
+    tg.quantize_fp8(x, q[:R], sf[:R], index=None if index is None else torch.tensor(index, dtype=torch.int32, device=dev))
+    _done()
+    for lo in range(0, K, step):
+        hi = min(K, lo + step)
+        want_q, want_sf = _rows_formula(x[:, lo:hi])
+        at = slice(lo // 128, X.blocks(hi))
+        for r in range(R):
+            none = index is not None and index[r] < 0
+            assert torch.equal(sf[r, at], torch.full_like(want_sf[0], X.FLOOR) / torch.full_like(want_sf[0], 448.0) if none else want_sf[0])
+            assert (q[r, lo:hi] == 0).all() if none else torch.equal(q[r, lo:hi], want_q[0])
+        assert (q[R, lo:hi] == 99).all()
+    assert (sf[R] == -1.0).all()
