@@ -68,7 +68,7 @@ gemm_status_t run(const Operands& o, Fp8Params p, cudaStream_t stream, int sms, 
         seen_units[dev].store(units, std::memory_order_release);
     }
     p.num_m = static_cast<int>((o.rows_a + Cfg::TM - 1) / Cfg::TM);
-    p.num_n = (p.N + Cfg::TN - 1) / Cfg::TN;
+    p.num_n = static_cast<int>((int64_t(p.N) + Cfg::TN - 1) / Cfg::TN);
     const long long tiles = static_cast<long long>(p.num_m) * p.num_n;
     if (tiles > 0x7fffffffLL / 8) return GEMM_ERR_INVALID_ARG;
     const long long row = static_cast<long long>(p.nkb) * 128;

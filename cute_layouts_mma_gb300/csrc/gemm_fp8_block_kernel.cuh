@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     auto scale_role = [&]() {
         griddep_wait();
         constexpr int LINES = 32 / KC;
-        const int nbs = (p.N + 127) >> 7;
+        const int nbs = static_cast<int>((static_cast<uint32_t>(p.N) + 127u) >> 7);
         const int line = lane / KC;
         int slot = 0;
         uint32_t ph = 0;

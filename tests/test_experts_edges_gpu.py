@@ -57,6 +57,41 @@ def test_gemm_another_c_and_infinite_rows_at_a_column_remainder(M, N, K, scales)
         assert (D[M:] == 12345.0).all()
 
 
+@pytest.mark.parametrize("scales", ["tiles", "rows"])
+def test_gemm_of_nearly_two_to_the_31_columns(scales):
+    """One row through the widest layer: narrow tiles, and (a scale per row of both) 128 x 128.
+    Integer codes and power-of-two scales: sums of 16 products below 2^8 are exact in bf16."""
+    dev = _dev()
+    if torch.cuda.mem_get_info(dev)[0] < 80 << 30:
+        pytest.skip("34 GB of weights")
+    N, K, step = 2 ** 31 - 8, 16, 1 << 24
+    g = torch.Generator(device=dev).manual_seed(5)
+    code = torch.tensor([0x00, 0x38, 0x40, 0xB8, 0xC0], dtype=torch.uint8, device=dev)  # 0, 1, 2, -1, -2
+    value = code.view(torch.float8_e4m3fn).float()
+    pick = torch.randint(0, 5, (1, K), generator=g, device=dev)
+    A, a = code[pick], value[pick]
+    B = torch.empty(N, K, dtype=torch.uint8, device=dev)
+    for lo in range(0, N, step):
+        hi = min(N, lo + step)
+        B[lo:hi] = code[torch.randint(0, 5, (hi - lo, K), generator=g, device=dev, dtype=torch.int32)]
+    count = N if scales == "rows" else X.blocks(N)
+    SFB = torch.empty(count, 1, device=dev)
+    for lo in range(0, count, step):
+        hi = min(count, lo + step)
+        SFB[lo:hi, 0] = 2.0 ** (torch.arange(lo, hi, device=dev) % 5).float()
+    SFA = torch.full((1, 1), 0.5, device=dev)
+    D = torch.full((2, N), 77.0, dtype=torch.bfloat16, device=dev)
+    tg.gemm_fp8_block(A, SFA, B, SFB, None, D[:1])
+    _done()
+    for lo in range(0, N, step):
+        hi = min(N, lo + step)
+        sums = (B[lo:hi].view(torch.float8_e4m3fn).float() * a).sum(dim=1)
+        n = torch.arange(lo, hi, device=dev)
+        want = 0.5 * sums * 2.0 ** ((n if scales == "rows" else n // 128) % 5).float()
+        assert torch.equal(D[0, lo:hi].float(), want)
+        assert (D[1, lo:hi] == 77.0).all()
+
+
 # ------------------------------------------------------------------ grouping
 
 @pytest.mark.parametrize("n", [2 ** 31 - 1, 2 ** 31 - 400, 2 ** 31 - 513])
