@@ -159,6 +159,10 @@ bool sizes_ok(int64_t M, int64_t N, int64_t K) {
     return M >= 0 && M < kLimit && N >= 1 && N < kLimit && K >= 1 && K < kLimit;
 }
 
+// Rows of A, and of B over all experts, of a grouped product: an expert's tiles begin at any row
+// and the last one reaches up to 255 rows past its end, within an int still.
+constexpr int64_t kMaxGroupedRows = (int64_t(1) << 31) - 512;
+
 }  // namespace
 
 unsigned int read_clear_error_fp8_block() { return read_clear_word(g_err_fp8_block); }
@@ -215,7 +219,7 @@ gemm_status_t gemm_fp8_block_grouped(int64_t R, int64_t N, int64_t K, int64_t E,
                                      const void* B, const float* SFB, const int32_t* offsets, void* D,
                                      cudaStream_t stream) {
     using namespace tn;
-    if (!sizes_ok(R, N, K) || E < 1 || E > kMaxExperts || E * N >= (int64_t(1) << 31)) return GEMM_ERR_INVALID_ARG;
+    if (!sizes_ok(R, N, K) || E < 1 || E > kMaxExperts || R > kMaxGroupedRows || E * N > kMaxGroupedRows) return GEMM_ERR_INVALID_ARG;
     if (K % 16 != 0 || N % 8 != 0) return GEMM_ERR_ALIGNMENT;
     if (R == 0) return GEMM_OK;
     if (A == nullptr || SFA == nullptr || B == nullptr || SFB == nullptr || offsets == nullptr || D == nullptr) return GEMM_ERR_INVALID_ARG;

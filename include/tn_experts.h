@@ -133,8 +133,8 @@ gemm_status_t gemm_fp8_block(int64_t M, int64_t N, int64_t K, const void *A, con
  * through B[e].  A u8[R][K], SFA float[R][ceil(K/128)], B u8[E][N][K],
  * SFB float[E][ceil(N/128)][ceil(K/128)], offsets int32[E+1] in device memory,
  * D bf16[R][N].  Rows outside every expert (from offsets[E] on) are not written; offsets
- * are read as if clamped to 0 .. R and made ascending.  1 <= E <= 1024; R >= 0;
- * E * N < 2^31; sizes and alignment otherwise as gemm_fp8_block.
+ * are read as if clamped to 0 .. R and made ascending.  1 <= E <= 1024; 0 <= R <= 2^31 - 512;
+ * E * N <= 2^31 - 512; sizes and alignment otherwise as gemm_fp8_block.
  */
 gemm_status_t gemm_fp8_block_grouped(int64_t R, int64_t N, int64_t K, int64_t E, const void *A, const float *SFA,
                                      const void *B, const float *SFB, const int32_t *offsets, void *D,
