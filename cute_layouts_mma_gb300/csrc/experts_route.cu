@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, VPT == 16 && LPT == 16 ? 4 :
     auto slot = [&](int l, int i) { return l * VPT + (VPT < 4 ? i : 4 * ((i / 4) ^ (l & (NV - 1))) + i % 4); };
     const int e0 = gl * VPT;
     const bool with_bias = p.bias != nullptr;
-    const bool need_total = !SIGMOID && (with_bias || !p.renormalize);
+    const bool need_total = !SIGMOID && (with_bias || !p.renormalize);  // of the keys, or of the weights
     const int size = p.E / p.groups, lanes = size / VPT;  // experts, lanes of a run
     const bool cut = p.groups > 1 && p.top_groups < p.groups;
     // runs of a power of two of whole lanes; others go through the table (LPT = 32 alone)
@@ -314,13 +314,15 @@ __global__ void __launch_bounds__(kRouteWarps * 32, VPT == 16 && LPT == 16 ? 4 :
 
     // weights of the picks: the chosen logits are read again
     float s = 0.0f;
-    if (gl < p.top_k) {
-        const float v = clean(to_f32(row[id]));
-        if (SIGMOID)
-            s = sigmoid(v);
-        else
-            s = exp_below(v, m);
-        if (need_total) s = total > 0.0f ? s / total : 0.0f;
+    const float v = gl < p.top_k ? clean(to_f32(row[id])) : neg_inf();
+    if (SIGMOID) {
+        if (gl < p.top_k) s = sigmoid(v);
+    } else if (p.renormalize) {
+        // shares of the chosen alone, below their own maximum (the gradient's way too): the row's
+        // may be of an expert that the bias or the runs passed over, far above all of them
+        s = exp_below(v, with_bias || cut ? group_max<LPT>(v) : m);
+    } else {
+        s = total > 0.0f ? exp_below(v, m) / total : 0.0f;
     }
     float w = s * p.scale;
     if (p.renormalize) {

@@ -34,7 +34,9 @@ enum { ROUTE_SIGMOID = 0, ROUTE_SOFTMAX = 1 };               /* scoring of exper
  *   ids[t][.]     = the top_k experts with the largest keys, in descending order, the
  *                   lower index first among equal keys.
  *   weights[t][j] = scale * s_j / sum_i s_i over the chosen (renormalize != 0; 0 where
- *                   that sum is 0), or scale * s_j.
+ *                   that sum is 0), or scale * s_j.  Renormalised shares of a softmax are
+ *                   exp(x_j - max of the chosen x) over their sum, however far the chosen
+ *                   lie below the row's largest.
  *
  * A logit of -inf masks its expert: it is chosen only when nothing else is left in the
  * kept runs, its weight is 0, and it adds nothing to its run's score (a run of masked

@@ -92,6 +92,59 @@ def test_gemm_of_nearly_two_to_the_31_columns(scales):
         assert (D[1, lo:hi] == 77.0).all()
 
 
+# ------------------------------------------------------------------ routing
+
+@pytest.mark.parametrize("T", [3, 2600, 13000])
+@pytest.mark.parametrize("E,groups", [(24, 1), (64, 1), (64, 4), (128, 1), (256, 8), (384, 1)])
+@pytest.mark.parametrize("above", [30.0, 95.0, 120.0, 3e38])
+def test_softmax_weights_of_experts_far_below_the_largest(T, E, groups, above):
+    """A bias chooses among experts far below the row's largest logit: the renormalised weights
+    are those of the chosen alone, and the gradient is theirs.  Bounds as for other routings:
+    exponentials and sums of a few 2^-23 each, and one rounding of a difference below 8."""
+    dev = _dev()
+    g = torch.Generator().manual_seed(T + E)
+    k, scale = 4, 2.5
+    x = torch.rand(T, E, generator=g) * 8 - 4
+    x[:, 5] = above
+    bias = torch.zeros(E)
+    bias[-6:] = 2.0 + torch.rand(6, generator=g)
+    w = torch.empty(T, k, device=dev)
+    ids = torch.empty(T, k, dtype=torch.int32, device=dev)
+    tg.expert_route(x.to(dev), bias.to(dev), w, ids, tg.ROUTE_SOFTMAX, groups=groups, top_groups=max(1, groups // 2), group_best=1, scale=scale)
+    dw = torch.randn(T, k, generator=g)
+    dx = torch.empty(T, E, device=dev)
+    tg.expert_route_grad(x.to(dev), ids, dw.to(dev), dx, tg.ROUTE_SOFTMAX, scale=scale)
+    _done()
+    ids = ids.cpu().long()
+    assert torch.equal(ids, bias.sort(descending=True).indices[:k].expand(T, k))
+    e = x.double().gather(1, ids).softmax(dim=1)
+    want = scale * e
+    assert ((w.cpu().double() - want).abs() <= want * (16 + E ** 0.5) * 2.0 ** -23).all()
+    dot = (dw.double() * e).sum(dim=1, keepdim=True)
+    grad = torch.zeros(T, E, dtype=torch.float64).scatter_(1, ids, want * (dw.double() - dot))
+    lim = scale * dw.abs().amax(dim=1, keepdim=True).double() * (k + E ** 0.5 + 16) * 2.0 ** -23
+    assert ((dx.cpu().double() - grad).abs() <= lim + grad.abs() * 2.0 ** -24).all()
+
+
+def test_softmax_weights_of_masked_choices_stay_zero():
+    """Chosen by the bias or for want of others, but masked: weight 0, beside ones that are not."""
+    dev = _dev()
+    x = torch.full((3, 16), -float("inf"))
+    x[1, 2], x[1, 9] = -200.0, -201.0
+    x[2, 4] = float("inf")
+    bias = torch.zeros(16)
+    bias[9] = 1.0
+    w = torch.empty(3, 4, device=dev)
+    ids = torch.empty(3, 4, dtype=torch.int32, device=dev)
+    tg.expert_route(x.to(dev), bias.to(dev), w, ids, tg.ROUTE_SOFTMAX)
+    _done()
+    assert (w[0] == 0).all()
+    assert ids[1, :2].tolist() == [9, 2] and (w[1, 2:] == 0).all()
+    want = torch.tensor([-201.0, -200.0], dtype=torch.float64).softmax(dim=0)
+    assert ((w[1, :2].cpu().double() - want).abs() <= 2.0 ** -19).all()
+    assert ids[2, 0].item() == 4 and w[2].tolist() == [1.0, 0.0, 0.0, 0.0]
+
+
 # ------------------------------------------------------------------ grouping
 
 @pytest.mark.parametrize("n", [2 ** 31 - 1, 2 ** 31 - 400, 2 ** 31 - 513])
