@@ -9,6 +9,7 @@ from __future__ import annotations
 import concurrent.futures as cf
 import glob
 import os
+import re
 import subprocess
 import sys
 
@@ -59,6 +60,24 @@ def up_to_date(variant: str = "") -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
+# Instances of the block-scaled FP8 kernel whose promotion warps hold 128 sums a thread (256
+# columns over two groups of four warps): they share out the registers that the launch holds,
+# so the compiler must have given each thread these (Fp8Config::kRegsLaunch).
+SPLIT_REGS = 168
+_SPLIT = re.compile(r"Compiling entry function '(\w*gemm_fp8_block_kernel\w*Fp8ConfigILi\d+ELi\d+ELi256E(?:Li\d+E){3}Li8E\w*)'"
+                    r".*?Used (\d+) registers", re.S)
+
+
+def check_register_split(log: str) -> int:
+    """Number of register-splitting instances in a compiler log (-Xptxas -v); raises if one of
+    them has another register count than its split needs, as every launch of it would be refused."""
+    found = _SPLIT.findall(log)
+    for name, regs in found:
+        if int(regs) != SPLIT_REGS:
+            raise RuntimeError(f"{name}: {regs} registers, its split of them needs {SPLIT_REGS}")
+    return len(found)
+
+
 def build(force: bool = False, verbose: bool = False, variant: str = "") -> str:
     """Build the library (variant "" is the product; others are test builds)."""
     lib = lib_path(variant)
@@ -75,6 +94,8 @@ def build(force: bool = False, verbose: bool = False, variant: str = "") -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
+        if os.path.basename(src) == "gemm_fp8_block.cu" and check_register_split(r.stderr) == 0:
+            raise RuntimeError(f"no register counts in the compiler's log of {src}")
         return obj, r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=len(_sources())) as ex:

@@ -56,6 +56,7 @@ gemm_status_t run(const Operands& o, Fp8Params p, cudaStream_t stream, int sms, 
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES) != cudaSuccess) return GEMM_ERR_CUDA;
         if (Cfg::kRegSplit) {
             // the promotion warps' registers come from what the launch holds and the others give up
+            // (another count, at which they would wait for ever, already fails the build: build.py)
             cudaFuncAttributes fa{};
             if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess || fa.numRegs != Cfg::kRegsLaunch) return GEMM_ERR_CUDA;
         }
