@@ -668,7 +668,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         // plus C, to D.  In fragments, each four of them are of one column of four: rows l / 4,
         // + 8, + 16, + 24.
         // staged_c: C's first boxes are in the staging buffers, or on their way (fetch_c).
-        const bool add = p.f32_out && p.C == p.D;  // the copy engine adds
+        // the copy engine adds: one addition and one rounding per element, subnormals kept (measured)
+        const bool add = p.f32_out && p.C == p.D;
         const bool c_boxes = Cfg::kBoxC && p.C != nullptr && !add;
         const int box_cols = p.f32_out ? 32 : 64;
         uint32_t cph = 0;  // parity of each buffer's C barrier

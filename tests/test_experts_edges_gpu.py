@@ -92,6 +92,29 @@ def test_gemm_of_nearly_two_to_the_31_columns(scales):
         assert (D[1, lo:hi] == 77.0).all()
 
 
+@pytest.mark.parametrize("M,N,K", [(3, 136, 272), (100, 264, 4112), (300, 1032, 400), (2050, 2056, 1168), (4100, 4104, 1040)])
+@pytest.mark.parametrize("scales", ["tiles", "rows"])
+def test_gemm_in_place_keeps_subnormals(M, N, K, scales):
+    """Sums, C and their totals below 2^-126, added in place (by the copy engine, where tiles
+    leave in boxes) and to another C: exact either way, in units of 2^-149."""
+    dev = _dev()
+    g = torch.Generator().manual_seed(M + N)
+    A, B = _integer_codes((M, K), g).to(dev), _integer_codes((N, K), g).to(dev)
+    kb = X.blocks(K)
+    SFA = torch.full((M, kb), 2.0 ** -70, device=dev)
+    SFB = torch.full((N if scales == "rows" else X.blocks(N), kb), 2.0 ** -79, device=dev)
+    C = (torch.randint(-2 ** 22, 2 ** 22, (M, N), generator=g).double() * 2.0 ** -149).float().to(dev)
+    want = A.double() @ B.double().t() * 2.0 ** -149 + C.double()
+    assert want.abs().max() < 2.0 ** -126 and (want != 0).any()
+    D = torch.full_like(C, 9.0)
+    tg.gemm_fp8_block(A, SFA, B, SFB, C, D)
+    _done()
+    assert torch.equal(D.double(), want)
+    tg.gemm_fp8_block(A, SFA, B, SFB, C, C)
+    _done()
+    assert torch.equal(C.double(), want)
+
+
 # ------------------------------------------------------------------ routing
 
 @pytest.mark.parametrize("T", [3, 2600, 13000])
