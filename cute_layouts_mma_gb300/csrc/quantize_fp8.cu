@@ -40,7 +40,8 @@ __device__ __forceinline__ void clear(Eight<T>& x) {
     for (int i = 0; i < static_cast<int>(sizeof(x) / 16); ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// X is streamed: read once, kept from evicting what the next kernels read.
+// X through the read-only path, in 16-byte loads.  (No eviction hint: gathered rows are read once
+// per row that asks for them, and that is from L2.)
 template <class T>
 __device__ __forceinline__ void load_eight(Eight<T>& x, const T* p) {
     uint4* w = reinterpret_cast<uint4*>(&x);

@@ -42,10 +42,10 @@ enum { ROUTE_SIGMOID = 0, ROUTE_SOFTMAX = 1 };               /* scoring of exper
  * kept runs, its weight is 0, and it adds nothing to its run's score (a run of masked
  * experts alone comes last).  NaN counts as -inf.  Scores and sums are fp32.
  *
- *   T >= 0, 1 <= E <= 1024, 1 <= top_k <= 32, 1 <= groups <= 32 with E % groups == 0,
+ *   0 <= T < 2^31, 1 <= E <= 1024, 1 <= top_k <= 32, 1 <= groups <= 32 with E % groups == 0,
  *   top_k <= top_groups * E / groups.
  *   logits   [T] rows of E elements of `dtype` (GEMM_DT_*), ld elements apart
- *            (ld >= E); aligned to its element.
+ *            (E <= ld < 2^31); aligned to its element.
  *   bias     float[E] or NULL.
  *   weights  float[T][top_k].       ids  int32[T][top_k].   (4-byte aligned)
  */
@@ -63,8 +63,8 @@ gemm_status_t expert_route(int64_t T, int64_t E, int64_t top_k, const void *logi
  *   ROUTE_SOFTMAX  dlogits_e = s_e (ds_e - sum_j ds_j s_j), ds_e = 0 where not chosen
  * rounded once to `dtype`.  An id outside 0 .. E-1 stands for no expert and is skipped;
  * the ids of a token are distinct.
- *   dlogits  [T] rows of E elements of `dtype`, ldd elements apart (the elements between
- *            rows are not written).
+ *   dlogits  [T] rows of E elements of `dtype`, ldd elements apart (E <= ldd < 2^31; the
+ *            elements between rows are not written).
  */
 gemm_status_t expert_route_grad(int64_t T, int64_t E, int64_t top_k, const void *logits, int64_t ld, int dtype,
                                 const int32_t *ids, const float *dweights, void *dlogits, int64_t ldd, int scoring,
@@ -87,7 +87,9 @@ gemm_status_t expert_group(int64_t T, int64_t top_k, int64_t E, const int32_t *i
 /*
  * FP8 E4M3 codes with one fp32 scale per block of 128 elements:
  *   a   = max(largest |x| of the block, 2^-100)
- *   SF  = a / 448,   Q = round_e4m3(x * (448 / a)), to nearest even.
+ *   SF  = a / 448,   Q = round_e4m3(x * (448 / a)), to nearest even,
+ * each operation rounded to fp32: a code is the nearest of x / SF except where x / SF lies
+ * within 2^-22 of its value from the middle of two codes, which may go either way.
  * (The lower bound on a keeps both factors finite; a block of zeros gets codes 0.)  A NaN
  * keeps its own code NaN and does not enter the block's maximum; a block with an
  * infinity gets an infinite scale and dequantises to NaN.
@@ -104,9 +106,10 @@ gemm_status_t expert_group(int64_t T, int64_t top_k, int64_t E, const int32_t *i
  *   layout FP8_TILES_T  the same blocks, codes and scales transposed:
  *                       Q u8[K][P], SF float[ceil(K/128)][ceil(P/128)].  K % 8 == 0.
  *
- *   M rows of X of K elements of `dtype`, ld elements apart (ld >= K; ld * element size a
+ *   M rows of X of K elements of `dtype`, ld elements apart (K <= ld < 2^31; ld * element size a
  *   multiple of 16).  R rows out (FP8_ROWS; else R is ignored).  `index` int32[R] or
- *   NULL; index_div >= 1.  SF and index 4-byte aligned.  K >= 1; M, R >= 0.
+ *   NULL; index_div >= 1.  SF and index 4-byte aligned.  1 <= K < 2^31 - 128;
+ *   0 <= M, R < 2^31, and M <= 65535 * 128 in the layouts other than FP8_ROWS.
  */
 enum { FP8_ROWS = 0, FP8_COLS = 1, FP8_TILES = 2, FP8_TILES_T = 3 };
 gemm_status_t quantize_fp8(int64_t M, int64_t K, const void *X, int64_t ld, int dtype, int layout, int64_t R,
