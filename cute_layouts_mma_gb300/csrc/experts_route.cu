@@ -9,9 +9,9 @@
 // lowest lane first and the lowest index within it is the lowest index among equal keys.
 // The kernel is bound by its instructions.  Per token of 256 fp32 logits, sigmoid, bias, top 8
 // of 4 of 8 groups (32768 tokens): 1300 instructions and 45 us taking picks out of unsorted
-// lists; 1130 and 36 us with sorted lists and a warp per token; 763 and 30 us with 16 lanes
-// per token, where the steps across lanes serve two tokens at once, and four blocks per SM
-// (the schedulers issue in 71 % of the cycles; the 36 MB would take 5 us).
+// lists; 1130 with sorted lists and a warp per token (32.1 us in the present kernel); 763 and
+// 29.5 us with 16 lanes per token, where the steps across lanes serve two tokens at once, and
+// four blocks per SM (the schedulers issue in 71 % of the cycles; the 36 MB would take 5 us).
 // Eight lanes need 555 but 128 registers (34 us); they are used up to 128 experts.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -458,7 +458,7 @@ cudaError_t launch_width(const RouteParams& p, int scoring, bool grad, int sms, 
     // several rounds of them (a token's own time is longer on fewer lanes).  A warp, 8 or 16
     // lanes per token (us): 64 experts, 4096 tokens 4.4, 4.4, 16384 tokens 9.6, 6.9; 128 experts,
     // 8192 tokens 6.8, 8.5, 12288 tokens 9.3, 9.2, 32768 tokens 20.3, 14.2; 256 experts in 8
-    // groups, 8192 tokens 10.0, 10.7, 14336 tokens 15.5, 14.9, 32768 tokens 31.9, 29.7.
+    // groups, 8192 tokens 10.0, 10.7, 14336 tokens 15.5, 14.9, 32768 tokens 32.1, 29.5.
     auto narrow = [&](int vpt) {
         const int size = p.E / p.groups, lanes = size / vpt;
         const bool whole = p.groups == 1 || p.top_groups == p.groups || (size % vpt == 0 && (lanes & (lanes - 1)) == 0);

@@ -27,10 +27,11 @@
 // loads 140 (257), and the store waits for the sums; so all else is kept off these warps.
 // Scales read lane by lane from global memory took 75 of 303 us (8192 x 8192 x 4096),
 // copied by these warps with cp.async 60; hence the ring and its warp.
-// 8192 x 8192 x 4096, bf16: 180 us, 3.05 PFLOP/s (8192^3 on normal values 403 us, 2.73 PFLOP/s
-// at the power limit, ~1690 MHz).  Builds that skip work: no additions and TMEM loads 159 us, no
-// store either 135, no operand loads either 125; the MMAs alone are 119.  The same of 4096 x 8192
-// x 4096 with a scale per row and column, fp32: 140, 95, 71, 67, 60.  No one part bounds it.
+// 8192 x 8192 x 4096, bf16: 177 us on codes of -1 to 1 (3.11 PFLOP/s), 190 to 194 on normal
+// values, whose power takes the clock down (8192^3, new inputs each pass: 403 to 419 us, 2.62 to
+// 2.73 PFLOP/s at ~1690 MHz).  Builds that skip work, at 180 us: no additions and TMEM loads 159,
+// no store either 135, no operand loads either 125; the MMAs alone are 119.  The same of 4096 x
+// 8192 x 4096 with a scale per row and column, fp32: 140, 95, 71, 67, 60.  No one part bounds it.
 // Work: persistent units over whole tiles, or, for few tiles, a cluster of 2, 4 or 8 CTAs
 // per tile that share its k-blocks and add their sums through distributed shared memory.
 // Every wait is bounded, as in the other kernels of the library.
@@ -117,7 +118,8 @@ struct Fp8Config {
     // Staging of the store (rows of A), and of C before it: boxes of 32 rows x 128 bytes per
     // promotion warp, 128B swizzle; as many as its columns take in bf16.  C's first boxes come
     // while the tile is summed.  4096 x 8192 x 8208 with a scale per row and column, fp32:
-    // without C 266 us, added in place 273, another C 294 (318 read by the lanes at the store).
+    // without C 266 to 281 us, added in place 273 to 285, another C 291 to 304 (318 read by the
+    // lanes at the store).
     static constexpr int OFF_STG = OFF_COL + STAGES * COL_BYTES;
     static constexpr int STG_BUFS = W > 64 ? 2 : 1;
     static constexpr int STG_WARP = kSwap ? 0 : STG_BUFS * 4096;

@@ -2,9 +2,9 @@
 // rows), along columns with the output transposed, and in tiles of 128 x 128.
 //
 // All forms read X once and write one byte per element; they are bound by HBM (columns of 8200
-// x 8192 bf16: 204 MB in 39 us, 78 % of the copy bandwidth) and, gathered rows, which come
+// x 8192 bf16: 204 MB in 38.6 us, 79 % of the copy bandwidth; tiles 32, transposed tiles 35) and, gathered rows, which come
 // from L2, by the SM's own work (32768 rows of 4096 out of 4096: 268 MB read there and 139 MB
-// written in 42 us).
+// written in 40.6 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -111,7 +111,7 @@ __device__ __forceinline__ float2 mul2(float2 a, float f) {
 // divisions of a block are made once, by the lanes that hold it, instead of by all of them.
 // Rows lie along grid.x and their segments of U pieces along grid.y, so that no index is
 // divided.  Bound by instructions next to HBM: 23 per element and 117 us with a maximum
-// and a division per lane, 7 and 42 us so (32768 x 4096 bf16 gathered).
+// and a division per lane, 7 and 41 us so (32768 x 4096 bf16 gathered).
 template <class T, int U>
 __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsParams p) {
     static_assert(U == 1 || U == 2 || U == 4 || U == 8, "pieces per segment");
